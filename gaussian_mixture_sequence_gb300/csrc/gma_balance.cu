@@ -582,7 +582,8 @@ __global__ void __launch_bounds__(kXThreads)
         int terms = 0;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const bool in = !(fabsf(d[j]) <= cut);   // a NaN stays
+            // a NaN stays; lanes past K have no term (theirs is 0, but NaN beside a NaN or an infinite factor)
+            const bool in = lane + 32 * j < K && !(fabsf(d[j]) <= cut);
             const unsigned m = __ballot_sync(0xffffffffu, in);
             if (in) {
                 list[terms + __popc(m & below)] = make_float2(d[j], __int_as_float(lane + 32 * j));
