@@ -189,10 +189,19 @@ def _params(shape, mu, var_raw, logit_pi, dev):
                    _ptr(logit_pi, "logit_pi", (H, K), torch.float32, dev))
 
 
-def _ws(shape, op, ws, dev):
+def _alloc(need, dev, stream):
+    """A workspace from torch's allocator, taken on the stream that will use it (default: the current one):
+    a block that another stream freed may still be read or written by what is queued there."""
+    if stream is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+
+
+def _ws(shape, op, ws, dev, stream):
     need = gma_workspace_size(shape, op)
     if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        ws = _alloc(need, dev, stream)
     return _ptr(ws, "ws", dtype=torch.uint8, device=dev), ws.numel()
 
 
@@ -208,7 +217,7 @@ def gma_responsibilities(shape: Shape, mu, var_raw, logit_pi, x, gamma, ws=None,
     xp = _ptr(x, "x", (s.B, s.H, s.N, s.d_route), _TORCH_DT[s.x_dtype], dev)
     gp = _ptr(gamma, "gamma", (s.B, s.H, s.N, s.K), torch.float32, dev)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_RESPONSIBILITIES, ws, dev)
+    wp, wn = _ws(s, OP_RESPONSIBILITIES, ws, dev, stream)
     _check("gma_responsibilities",
            load().gma_responsibilities(ctypes.byref(s), prm, xp, gp, wp, wn, _stream(dev, stream)))
     return gamma
@@ -227,7 +236,7 @@ def gma_responsibility_stats(shape: Shape, mu, var_raw, logit_pi, x, usage, coun
     ep = _ptr(entropy, "entropy", (s.H, 2), torch.float32, dev)
     ap = _ptr(assign, "assign", (s.B, s.H, s.N), torch.int32, dev, optional=True)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_USAGE, ws, dev)
+    wp, wn = _ws(s, OP_USAGE, ws, dev, stream)
     _check("gma_responsibility_stats",
            load().gma_responsibility_stats(ctypes.byref(s), prm, xp, up, cp, ep, ap, wp, wn, _stream(dev, stream)))
     return usage, counts, entropy
@@ -249,7 +258,7 @@ def gma_backward(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, dout, dqx, dkx,
     dr = _ptr(dvar_raw, "dvar_raw", (s.H, s.K, s.d_route), f32, dev)
     dl = _ptr(dlogit_pi, "dlogit_pi", (s.H, s.K), f32, dev)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_BACKWARD, ws, dev)
+    wp, wn = _ws(s, OP_BACKWARD, ws, dev, stream)
     _check("gma_backward",
            load().gma_backward(ctypes.byref(s), int(bool(causal)), prm, q, k, vv, g, dq, dk, dvp, dm, dr, dl, wp, wn,
                                _stream(dev, stream)))
@@ -272,9 +281,8 @@ def gma_forward_cross(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, out, ws=No
     vv = _ptr(v, "v", (s.B, s.H, n_kv, s.d_v), vdt, dev)
     o = _ptr(out, "out", (s.B, s.H, s.N, s.d_v), torch.float32, dev)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    need = gma_cross_workspace_size(s, n_kv)
     if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        ws = _alloc(gma_cross_workspace_size(s, n_kv), dev, stream)
     wp = _ptr(ws, "ws", dtype=torch.uint8, device=dev)
     _check("gma_forward_cross",
            load().gma_forward_cross(ctypes.byref(s), n_kv, prm, q, k, vv, o, wp, ws.numel(), _stream(dev, stream)))
@@ -294,7 +302,7 @@ def gma_forward_bidir(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, out, ws=No
     dev = qx.device
     q, k, vv, o = _fwd_ptrs(shape, qx, kx, v, out, dev)
     prm = _params(shape, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(shape, OP_BIDIR, ws, dev)
+    wp, wn = _ws(shape, OP_BIDIR, ws, dev, stream)
     _check("gma_forward_bidir",
            load().gma_forward_bidir(ctypes.byref(shape), prm, q, k, vv, o, wp, wn, _stream(dev, stream)))
     return out
@@ -310,7 +318,7 @@ def gma_forward_causal(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, out, stat
     si = _ptr(state_in, "state_in", sshape, torch.float32, dev, optional=True)
     so = _ptr(state_out, "state_out", sshape, torch.float32, dev, optional=True)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_CAUSAL, ws, dev)
+    wp, wn = _ws(s, OP_CAUSAL, ws, dev, stream)
     _check("gma_forward_causal",
            load().gma_forward_causal(ctypes.byref(s), prm, q, k, vv, si, so, o, wp, wn, _stream(dev, stream)))
     return out
@@ -344,7 +352,7 @@ def gma_forward_causal_host(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, out,
     si = _ptr(state_in, "state_in", sshape, torch.float32, dev, optional=True)
     so = _ptr(state_out, "state_out", sshape, torch.float32, dev, optional=True)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_CAUSAL_HOST, ws, dev)
+    wp, wn = _ws(s, OP_CAUSAL_HOST, ws, dev, stream)
     _check("gma_forward_causal_host",
            load().gma_forward_causal_host(ctypes.byref(s), prm, q, k, vv, si, so, o, wp, wn, _stream(dev, stream)))
     return out
@@ -364,7 +372,7 @@ def gma_forward_causal_profiled(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, 
     si = _ptr(state_in, "state_in", sshape, torch.float32, dev, optional=True)
     so = _ptr(state_out, "state_out", sshape, torch.float32, dev, optional=True)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_CAUSAL, ws, dev)
+    wp, wn = _ws(s, OP_CAUSAL, ws, dev, stream)
     prof = _profile(events)
     _check("gma_forward_causal_profiled",
            load().gma_forward_causal_profiled(ctypes.byref(s), prm, q, k, vv, si, so, o, wp, wn,
@@ -387,7 +395,7 @@ def gma_forward_bidir_profiled(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, o
     dev = qx.device
     q, k, vv, o = _fwd_ptrs(shape, qx, kx, v, out, dev)
     prm = _params(shape, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(shape, OP_BIDIR, ws, dev)
+    wp, wn = _ws(shape, OP_BIDIR, ws, dev, stream)
     prof = _profile(events)
     _check("gma_forward_bidir_profiled",
            load().gma_forward_bidir_profiled(ctypes.byref(shape), prm, q, k, vv, o, wp, wn,
@@ -407,7 +415,7 @@ def gma_decode_step_profiled(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, sta
     st = _ptr(state, "state", (s.B, s.H, s.K * s.d_v + s.K), torch.float32, dev)
     o = _ptr(out, "out", (s.B, s.H, s.d_v), torch.float32, dev)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_DECODE, ws, dev)
+    wp, wn = _ws(s, OP_DECODE, ws, dev, stream)
     prof = _profile(events)
     _check("gma_decode_step_profiled",
            load().gma_decode_step_profiled(ctypes.byref(s), prm, q, k, vv, st, o, wp, wn, _stream(dev, stream),
@@ -426,7 +434,7 @@ def gma_decode_step(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, state, out, 
     st = _ptr(state, "state", (s.B, s.H, s.K * s.d_v + s.K), torch.float32, dev)
     o = _ptr(out, "out", (s.B, s.H, s.d_v), torch.float32, dev)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_DECODE, ws, dev)
+    wp, wn = _ws(s, OP_DECODE, ws, dev, stream)
     _check("gma_decode_step",
            load().gma_decode_step(ctypes.byref(s), prm, q, k, vv, st, o, wp, wn, _stream(dev, stream)))
     return out
@@ -488,11 +496,9 @@ def _p(t, name, shape, dtype, dev, optional=False):
 
 
 def _scratch(need, ws, dev, stream):
-    """The caller's workspace, or one from torch's allocator that stays alive for the call's stream."""
+    """The caller's workspace, or one of the call's stream."""
     if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        if stream is not None:
-            ws.record_stream(stream)
+        ws = _alloc(need, dev, stream)
     return _p(ws, "ws", ws.shape, torch.uint8, dev), ws.numel()
 
 
