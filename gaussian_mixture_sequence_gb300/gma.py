@@ -199,10 +199,12 @@ def _alloc(need, dev, stream):
 
 
 def _ws(shape, op, ws, dev, stream):
+    """Pointer, bytes and tensor of the workspace.  Callers hold the tensor until their launches are queued:
+    the library runs without the interpreter's lock, and another thread may allocate meanwhile."""
     need = gma_workspace_size(shape, op)
     if ws is None:
         ws = _alloc(need, dev, stream)
-    return _ptr(ws, "ws", dtype=torch.uint8, device=dev), ws.numel()
+    return _ptr(ws, "ws", dtype=torch.uint8, device=dev), ws.numel(), ws
 
 
 def _stream(dev, stream):
@@ -217,7 +219,7 @@ def gma_responsibilities(shape: Shape, mu, var_raw, logit_pi, x, gamma, ws=None,
     xp = _ptr(x, "x", (s.B, s.H, s.N, s.d_route), _TORCH_DT[s.x_dtype], dev)
     gp = _ptr(gamma, "gamma", (s.B, s.H, s.N, s.K), torch.float32, dev)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_RESPONSIBILITIES, ws, dev, stream)
+    wp, wn, ws = _ws(s, OP_RESPONSIBILITIES, ws, dev, stream)
     _check("gma_responsibilities",
            load().gma_responsibilities(ctypes.byref(s), prm, xp, gp, wp, wn, _stream(dev, stream)))
     return gamma
@@ -236,7 +238,7 @@ def gma_responsibility_stats(shape: Shape, mu, var_raw, logit_pi, x, usage, coun
     ep = _ptr(entropy, "entropy", (s.H, 2), torch.float32, dev)
     ap = _ptr(assign, "assign", (s.B, s.H, s.N), torch.int32, dev, optional=True)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_USAGE, ws, dev, stream)
+    wp, wn, ws = _ws(s, OP_USAGE, ws, dev, stream)
     _check("gma_responsibility_stats",
            load().gma_responsibility_stats(ctypes.byref(s), prm, xp, up, cp, ep, ap, wp, wn, _stream(dev, stream)))
     return usage, counts, entropy
@@ -258,7 +260,7 @@ def gma_backward(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, dout, dqx, dkx,
     dr = _ptr(dvar_raw, "dvar_raw", (s.H, s.K, s.d_route), f32, dev)
     dl = _ptr(dlogit_pi, "dlogit_pi", (s.H, s.K), f32, dev)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_BACKWARD, ws, dev, stream)
+    wp, wn, ws = _ws(s, OP_BACKWARD, ws, dev, stream)
     _check("gma_backward",
            load().gma_backward(ctypes.byref(s), int(bool(causal)), prm, q, k, vv, g, dq, dk, dvp, dm, dr, dl, wp, wn,
                                _stream(dev, stream)))
@@ -302,7 +304,7 @@ def gma_forward_bidir(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, out, ws=No
     dev = qx.device
     q, k, vv, o = _fwd_ptrs(shape, qx, kx, v, out, dev)
     prm = _params(shape, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(shape, OP_BIDIR, ws, dev, stream)
+    wp, wn, ws = _ws(shape, OP_BIDIR, ws, dev, stream)
     _check("gma_forward_bidir",
            load().gma_forward_bidir(ctypes.byref(shape), prm, q, k, vv, o, wp, wn, _stream(dev, stream)))
     return out
@@ -318,7 +320,7 @@ def gma_forward_causal(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, out, stat
     si = _ptr(state_in, "state_in", sshape, torch.float32, dev, optional=True)
     so = _ptr(state_out, "state_out", sshape, torch.float32, dev, optional=True)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_CAUSAL, ws, dev, stream)
+    wp, wn, ws = _ws(s, OP_CAUSAL, ws, dev, stream)
     _check("gma_forward_causal",
            load().gma_forward_causal(ctypes.byref(s), prm, q, k, vv, si, so, o, wp, wn, _stream(dev, stream)))
     return out
@@ -352,7 +354,7 @@ def gma_forward_causal_host(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, out,
     si = _ptr(state_in, "state_in", sshape, torch.float32, dev, optional=True)
     so = _ptr(state_out, "state_out", sshape, torch.float32, dev, optional=True)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_CAUSAL_HOST, ws, dev, stream)
+    wp, wn, ws = _ws(s, OP_CAUSAL_HOST, ws, dev, stream)
     _check("gma_forward_causal_host",
            load().gma_forward_causal_host(ctypes.byref(s), prm, q, k, vv, si, so, o, wp, wn, _stream(dev, stream)))
     return out
@@ -372,7 +374,7 @@ def gma_forward_causal_profiled(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, 
     si = _ptr(state_in, "state_in", sshape, torch.float32, dev, optional=True)
     so = _ptr(state_out, "state_out", sshape, torch.float32, dev, optional=True)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_CAUSAL, ws, dev, stream)
+    wp, wn, ws = _ws(s, OP_CAUSAL, ws, dev, stream)
     prof = _profile(events)
     _check("gma_forward_causal_profiled",
            load().gma_forward_causal_profiled(ctypes.byref(s), prm, q, k, vv, si, so, o, wp, wn,
@@ -395,7 +397,7 @@ def gma_forward_bidir_profiled(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, o
     dev = qx.device
     q, k, vv, o = _fwd_ptrs(shape, qx, kx, v, out, dev)
     prm = _params(shape, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(shape, OP_BIDIR, ws, dev, stream)
+    wp, wn, ws = _ws(shape, OP_BIDIR, ws, dev, stream)
     prof = _profile(events)
     _check("gma_forward_bidir_profiled",
            load().gma_forward_bidir_profiled(ctypes.byref(shape), prm, q, k, vv, o, wp, wn,
@@ -415,7 +417,7 @@ def gma_decode_step_profiled(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, sta
     st = _ptr(state, "state", (s.B, s.H, s.K * s.d_v + s.K), torch.float32, dev)
     o = _ptr(out, "out", (s.B, s.H, s.d_v), torch.float32, dev)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_DECODE, ws, dev, stream)
+    wp, wn, ws = _ws(s, OP_DECODE, ws, dev, stream)
     prof = _profile(events)
     _check("gma_decode_step_profiled",
            load().gma_decode_step_profiled(ctypes.byref(s), prm, q, k, vv, st, o, wp, wn, _stream(dev, stream),
@@ -434,7 +436,7 @@ def gma_decode_step(shape: Shape, mu, var_raw, logit_pi, qx, kx, v, state, out, 
     st = _ptr(state, "state", (s.B, s.H, s.K * s.d_v + s.K), torch.float32, dev)
     o = _ptr(out, "out", (s.B, s.H, s.d_v), torch.float32, dev)
     prm = _params(s, mu, var_raw, logit_pi, dev)
-    wp, wn = _ws(s, OP_DECODE, ws, dev, stream)
+    wp, wn, ws = _ws(s, OP_DECODE, ws, dev, stream)
     _check("gma_decode_step",
            load().gma_decode_step(ctypes.byref(s), prm, q, k, vv, st, o, wp, wn, _stream(dev, stream)))
     return out
@@ -496,10 +498,10 @@ def _p(t, name, shape, dtype, dev, optional=False):
 
 
 def _scratch(need, ws, dev, stream):
-    """The caller's workspace, or one of the call's stream."""
+    """_ws of the operators that size their workspaces themselves."""
     if ws is None:
         ws = _alloc(need, dev, stream)
-    return _p(ws, "ws", ws.shape, torch.uint8, dev), ws.numel()
+    return _p(ws, "ws", ws.shape, torch.uint8, dev), ws.numel(), ws
 
 
 def _run(fn, dev, stream, *args):
@@ -591,7 +593,7 @@ def gma_beam_select(shape: BeamShape, logits, score_in, score_out, parent, token
     fi = _p(finished_in, "finished_in", bw, torch.uint8, dev, optional=True)
     fo = _p(finished_out, "finished_out", bw, torch.uint8, dev, optional=True)
     need = gma_beam_workspace_size(s)
-    wp, wn = _scratch(need, ws, dev, stream) if need else (None, 0)
+    wp, wn, ws = _scratch(need, ws, dev, stream) if need else (None, 0, None)
     _run("gma_beam_select", dev, stream, ctypes.byref(s), lp, si, fi, so, pp, tp, fo, wp, wn)
     return score_out, parent, token
 
@@ -631,7 +633,7 @@ def gma_balance_loss(shape: Shape, mu, var_raw, logit_pi, x, gamma, loss, counts
     op = _p(loss, "loss", (s.H,), f32, dev)
     cp = _p(counts, "counts", (s.H, s.K), torch.int64, dev)
     pp = _p(prob, "prob", (s.H, s.K), f32, dev)
-    wp, wn = _scratch(gma_balance_workspace_size(s), ws, dev, stream)
+    wp, wn, ws = _scratch(gma_balance_workspace_size(s), ws, dev, stream)
     _run("gma_balance_loss", dev, stream, ctypes.byref(s), prm, xp, lp, gp, op, cp, pp, wp, wn)
     return loss, counts, prob
 
@@ -652,7 +654,7 @@ def gma_balance_backward(shape: Shape, mu, var_raw, logit_pi, x, gamma, counts, 
     op = _p(dloss, "dloss", (s.H,), f32, dev)
     g = (_p(dx, "dx", (s.B, s.H, s.N, s.d_route), f32, dev), _p(dmu, "dmu", (s.H, s.K, s.d_route), f32, dev),
          _p(dvar_raw, "dvar_raw", (s.H, s.K, s.d_route), f32, dev), _p(dlogit_pi, "dlogit_pi", (s.H, s.K), f32, dev))
-    wp, wn = _scratch(gma_balance_workspace_size(s), ws, dev, stream)
+    wp, wn, ws = _scratch(gma_balance_workspace_size(s), ws, dev, stream)
     _run("gma_balance_backward", dev, stream, ctypes.byref(s), prm, xp, lp, gp, cp, op, *g, int(bool(accumulate)), wp,
          wn)
     return dx, dmu, dvar_raw, dlogit_pi

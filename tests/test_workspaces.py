@@ -1,5 +1,6 @@
 """Workspaces that the binding takes from torch's allocator: on which stream, and for how long."""
 import contextlib
+import weakref
 
 import pytest
 import torch
@@ -25,23 +26,64 @@ def test_a_workspace_is_allocated_on_the_stream_of_the_call(monkeypatch):
     assert taken == [(100, "default"), (16, "side")] and current == ["default"]
 
 
-def _calls():
+class _Held:
+    """A library whose calls record whether the workspace that was handed out is still held."""
+
+    def __init__(self, block):
+        self.block, self.held = block, []
+
+    def __getattr__(self, name):
+        if name.endswith("_size"):
+            return lambda *a: 64
+
+        def call(*a):
+            self.held.append(self.block() is not None)
+            return 0
+        return call
+
+
+@pytest.mark.parametrize("name", ["responsibilities", "stats", "causal", "bidir", "cross", "backward", "decode", "beam",
+                                  "balance", "balance_backward"])
+def test_a_workspace_is_held_until_the_launches_are_queued(monkeypatch, name):
+    """On host tensors, with the library and the checks of pointers replaced."""
+    block = [lambda: None]
+
+    def alloc(need, dev, stream):
+        t = torch.empty(max(need, 16), dtype=torch.uint8)
+        block[0] = weakref.ref(t)
+        return t
+
+    lib = _Held(lambda: block[0]())
+    monkeypatch.setattr(gma, "_alloc", alloc)
+    monkeypatch.setattr(gma, "_lib", lib)
+    monkeypatch.setattr(gma, "load", lambda: lib)
+    monkeypatch.setattr(gma, "_ptr", lambda *a, **k: 16)
+    monkeypatch.setattr(gma, "_p", lambda *a, **k: 16)
+    monkeypatch.setattr(gma, "_device_index", lambda *a: 0)
+    monkeypatch.setattr(gma, "_current_device", lambda: 0)
+    monkeypatch.setattr(gma, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(gma, "_stream", lambda dev, stream: None)
+    _calls("cpu", small=True)[name][1](None)
+    assert lib.held == [True] and block[0]() is None
+
+
+def _calls(dev=DEV, small=False):
     """name -> (workspace bytes, call(stream)) of every kind of entry point that takes a workspace."""
-    g = torch.Generator(device=DEV).manual_seed(3)
-    mk = lambda *s: torch.randn(*s, device=DEV, generator=g)
-    B, H, N, D, K = 2, 2, 300, 64, 128
+    g = torch.Generator(device=dev).manual_seed(3)
+    mk = lambda *s: torch.randn(*s, device=dev, generator=g)
+    B, H, N, D, K = 2, 2, 3 if small else 300, 64, 128
     s = gma.Shape.make(B, H, N, D, 64, K)
     prm = (mk(H, K, D), mk(H, K, D), mk(H, K))
     q, k, v, out = mk(B, H, N, D), mk(B, H, N, D), mk(B, H, N, 64), mk(B, H, N, 64)
     gamma, rows = mk(B, H, N, K), [mk(B, H, N, D) for _ in range(3)]
     loss, prob, usage, ent = mk(H), mk(H, K), mk(H, K), mk(H, 2)
-    counts = torch.zeros(H, K, dtype=torch.int64, device=DEV)
+    counts = torch.zeros(H, K, dtype=torch.int64, device=dev)
     grads = [mk(*p.shape) for p in prm]
     state, tok, tout = mk(B, H, K * 64 + K), mk(B, H, 64), mk(B, H, 64)
-    bs = gma.BeamShape.make(16, 8, 40000)
-    logits, score = mk(16, 8, 40000), mk(16, 8)
-    sco, par, ids = mk(16, 8), torch.zeros(16, 8, dtype=torch.int32, device=DEV), torch.zeros(16, 8, dtype=torch.int32,
-                                                                                            device=DEV)
+    V = 40 if small else 40000
+    bs = gma.BeamShape.make(16, 8, V)
+    logits, score, sco = mk(16, 8, V), mk(16, 8), mk(16, 8)
+    par, ids = (torch.zeros(16, 8, dtype=torch.int32, device=dev) for _ in range(2))
     size = lambda op: gma.gma_workspace_size(s, op)
     return {
         "responsibilities": (size(gma.OP_RESPONSIBILITIES),
