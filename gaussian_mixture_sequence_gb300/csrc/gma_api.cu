@@ -1135,23 +1135,29 @@ extern "C" gma_status gma_beam_reorder(int B, int W, size_t row_bytes, const int
 // ---- the balance loss ----
 namespace {
 
-// The routing's scratch (as gma_responsibilities), then the loss's or the gradients' (shared).
+// The routing's scratch, then the loss's; the gradients' takes the place of both.  The routing is one that
+// evaluates every component: the bounded routing of K = 128 writes 0 for posteriors below e^-30, and a
+// head whose rows are all but one-hot has no others beside the best.
 struct BalPlan {
-    WsPlan w;
+    size_t prm, cst, img;
+    bool gtc;
     size_t prec, cst2, second, psum, pcnt, inv, terms, n_terms, hist, part, bytes;
 };
 
 BalPlan plan_balance(const Dims &dm)
 {
     BalPlan p;
-    p.w = plan(dm, GMA_OP_RESPONSIBILITIES);
-    size_t off = p.w.bytes;
+    size_t off = 0;
     auto take = [&](size_t n) {
         const size_t o = off;
         off = (size_t)round_up((long long)(off + n), 256);
         return o;
     };
     const size_t hk = (size_t)dm.H * dm.K, nb = (size_t)dm.H * balance_blocks(dm);
+    p.prm = take(hk * (dm.D / 2) * 16);
+    p.cst = take(hk * 4);
+    p.gtc = resp_gtc_fits(dm) && resp_gtc_output_ok(dm, dm.K, GL_F32);
+    p.img = take(p.gtc ? gtc_image_bytes(dm) : 0);
     p.prec = take(hk * dm.D * 8);
     p.cst2 = take(hk * 8);
     p.second = take((size_t)dm.H * 4);
@@ -1205,14 +1211,17 @@ extern "C" gma_status gma_balance_loss(const gma_shape *shape, gma_params params
     float2 *prec = at<float2>(ws, bp.prec), *cst2 = at<float2>(ws, bp.cst2);
     float *second = at<float>(ws, bp.second);
     if (dm.N > 0) {
-        const WsPlan &wp = bp.w;
-        float4 *prm = at<float4>(ws, wp.prm);
-        float *cst = at<float>(ws, wp.cst);
-        const PrunedImages img = images(ws, wp);
+        float4 *prm = at<float4>(ws, bp.prm);
+        float *cst = at<float>(ws, bp.cst);
+        unsigned char *img = at<unsigned char>(ws, bp.img);
         GMA_CUDA(launch_balance_prep(dm, params, prec, cst2, second, st));
-        GMA_CUDA(prep_routing(dm, params, prm, cst, wp, img, st));
-        GMA_CUDA(launch_resp(dm, prm, cst, routing_images(wp, img), x, gamma, dm.K, GL_F32, st, 0));
-        if (wp.pruned) GMA_CUDA(launch_resp_dense(dm, x, gamma, dm, nullptr, nullptr, img, GL_F32, st));
+        GMA_CUDA(launch_prep(dm, params, prm, cst, st));
+        if (bp.gtc) {
+            GMA_CUDA(launch_prep_gtc(dm, prm, cst, img, st));
+            GMA_CUDA(launch_resp_gtc(dm, img, prm, cst, x, gamma, dm.K, GL_F32, st));
+        } else {
+            GMA_CUDA(launch_resp(dm, prm, cst, nullptr, x, gamma, dm.K, GL_F32, st));
+        }
     }
     GMA_CUDA(launch_balance_loss(dm, params, x, lengths, prec, cst2, second, gamma, at<float>(ws, bp.psum),
                                  at<int>(ws, bp.pcnt), loss, counts, prob, st));

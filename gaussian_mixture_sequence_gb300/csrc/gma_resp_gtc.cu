@@ -1000,16 +1000,14 @@ int gtc_width(int K) { return K <= 32 ? 32 : (K <= 64 ? 64 : (K <= 128 ? 128 : (
 
 } // namespace
 
-bool resp_gtc_applies(const Dims &dm)
-{
-    return dm.D == kQD && dm.K >= 17 && dm.K <= 512 && !resp_pruned_applies(dm);
-}
+bool resp_gtc_fits(const Dims &dm) { return dm.D == kQD && dm.K >= 17 && dm.K <= 512; }
+bool resp_gtc_applies(const Dims &dm) { return resp_gtc_fits(dm) && !resp_pruned_applies(dm); }
 
-size_t gtc_image_bytes(const Dims &dm) { return resp_gtc_applies(dm) ? dm.H * gtc_pitch(gtc_width(dm.K)) : 0; }
+size_t gtc_image_bytes(const Dims &dm) { return resp_gtc_fits(dm) ? dm.H * gtc_pitch(gtc_width(dm.K)) : 0; }
 
 cudaError_t launch_prep_gtc(const Dims &dm, const float4 *prm, const float *cst, unsigned char *img, cudaStream_t st)
 {
-    if (!resp_gtc_applies(dm)) return cudaErrorInvalidValue;
+    if (!resp_gtc_fits(dm)) return cudaErrorInvalidValue;
     switch (gtc_width(dm.K)) {
     case 32: k_prep_gtc<32><<<dim3(dm.H, 1, 1), 32 * 4, 0, st>>>(dm.K, prm, cst, img); break;
     case 64: k_prep_gtc<64><<<dim3(dm.H, 1, 1), 64 * 4, 0, st>>>(dm.K, prm, cst, img); break;
@@ -1093,7 +1091,7 @@ cudaError_t launch_gtc(const Dims &dm, const unsigned char *img, const float4 *p
 cudaError_t launch_resp_gtc(const Dims &dm, const unsigned char *img, const float4 *prm, const float *cst,
                             const void *x, void *gamma, int ldg, int layout, cudaStream_t st)
 {
-    if (!resp_gtc_applies(dm) || !resp_gtc_output_ok(dm, ldg, layout)) return cudaErrorInvalidValue;
+    if (!resp_gtc_fits(dm) || !resp_gtc_output_ok(dm, ldg, layout)) return cudaErrorInvalidValue;
     switch (gtc_width(dm.K)) {
     case 32: return launch_gtc<32>(dm, img, prm, cst, x, gamma, ldg, layout, st);
     case 64: return launch_gtc<64>(dm, img, prm, cst, x, gamma, ldg, layout, st);

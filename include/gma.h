@@ -356,7 +356,8 @@ gma_status gma_beam_reorder(int B, int W, size_t row_bytes, const int *parent, v
  * evaluated with two fp32 values each, so that near ties are counted as in 64
  * bits (equal components: the lowest), gamma carries the rounding of an fp32
  * result (the posteriors below, up to 2^-23 of the scale), and the gradients of
- * heads whose rows are all but one-hot keep their relative accuracy.
+ * heads whose rows are all but one-hot keep their relative accuracy, down to
+ * the end of the fp32 range (posteriors below 2^-126 are 0).
  * A row with a NaN makes prob and loss NaN and is counted nowhere.
  * Sums run in a fixed order: repeated calls give identical results.  Workspace:
  * gma_balance_workspace_size(shape); shape->d_v, chunk, eps, v_dtype and
