@@ -940,13 +940,16 @@ extern "C" gma_status gma_backward(const gma_shape *shape, int causal, gma_param
 // ---- the gated recurrence ----
 namespace {
 
+// Rows of a sequence: positions are 32-bit, some 10^4 rows (a round of a cluster) past the last one included.
+constexpr int kMaxRows = 1 << 30;
+
 gma_status scan_dims(const gma_scan_shape *s, ScanDims *sd)
 {
     if (!s) return GMA_ERR_INVALID_ARG;
     if (s->B < 1 || s->H < 1 || s->N < 0 || s->D < 1) return GMA_ERR_INVALID_ARG;
     if ((unsigned)s->form > 1u || (unsigned)s->dtype > 1u) return GMA_ERR_INVALID_ARG;
     const long long S = (long long)s->B * s->H;
-    if (S > 65535 || s->D > 65536) return GMA_ERR_UNSUPPORTED;
+    if (S > 65535 || s->D > 65536 || s->N > kMaxRows) return GMA_ERR_UNSUPPORTED;
     if (S * (long long)(s->N > 0 ? s->N : 1) >= (1LL << 40) / s->D) return GMA_ERR_UNSUPPORTED;
     *sd = ScanDims{(int)S, s->H, s->N, s->D, s->form == GMA_SCAN_MEAN, s->dtype == GMA_BF16};
     return GMA_OK;

@@ -246,9 +246,9 @@ gma_status gma_decode_step(const gma_shape *shape, gma_params params, const void
  *   state_in      nullable [B, H, D] fp32: h before the first row (NULL: 0)
  *   state_out     nullable [B, H, D] fp32: h after the last row of each
  *                 sequence.  May be state_in itself.
- * Supported: 1 <= D <= 65536, B*H <= 65535, B*H*N*D < 2^40.  With N = 0 the
- * sequence pointers may be NULL and state_out is state_in (or 0).  A NaN gate
- * or input makes its channel NaN from there on.  No workspace.              */
+ * Supported: 1 <= D <= 65536, N <= 2^30, B*H <= 65535, B*H*N*D < 2^40.  With
+ * N = 0 the sequence pointers may be NULL and state_out is state_in (or 0).  A
+ * NaN gate or input makes its channel NaN from there on.  No workspace.     */
 typedef enum { GMA_SCAN_SUM = 0, GMA_SCAN_MEAN = 1 } gma_scan_form;
 
 typedef struct {

@@ -122,3 +122,15 @@ def test_binding_refuses_wrong_tensors():
             call()
     with pytest.raises(KeyError):
         gma.ScanShape.make(1, 1, 8, 16, form="product")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [1, 64])
+def test_rejects_sequences_whose_positions_would_pass_31_bits(lib, D, dtype):
+    for fn, names in _entries(lib)[:2]:
+        for N in ((1 << 30) + 1, (1 << 31) - 20000, (1 << 31) - 1):
+            assert _call(fn, names, gma.ScanShape.make(1, 1, N, D, dtype=dtype)) == 2
+        # 2^30 itself passes the shape's checks (the first pointer's alignment is what fails)
+        assert _call(fn, names, gma.ScanShape.make(1, 1, 1 << 30, 1, dtype=dtype), x=BASE + 4) == 3
+    one = gma.ScanShape.make(1, 1, (1 << 31) - 1, D, dtype=dtype)   # (not looked at by the step)
+    assert _call(lib.gma_gated_step, ONE, one, x=BASE + 4) == 3
