@@ -1138,6 +1138,13 @@ extern "C" gma_status gma_beam_reorder(int B, int W, size_t row_bytes, const int
 // ---- the balance loss ----
 namespace {
 
+// The walk over a head's rows adds two positions of a sequence in 32 bits.
+gma_status balance_dims(const gma_shape *shape, Dims *dm)
+{
+    GMA_TRY(make_dims(shape, dm, GMA_OP_RESPONSIBILITIES));
+    return dm->N > kMaxRows ? GMA_ERR_UNSUPPORTED : GMA_OK;
+}
+
 // The routing's scratch, then the loss's; the gradients' takes the place of both.  The routing is one that
 // evaluates every component: the bounded routing of K = 128 writes 0 for posteriors below e^-30, and a
 // head whose rows are all but one-hot has no others beside the best.
@@ -1184,7 +1191,7 @@ size_t row_bytes(const Dims &dm) { return (size_t)dm.BH() * dm.N * dm.D * (dm.x_
 extern "C" size_t gma_balance_workspace_size(const gma_shape *shape)
 {
     Dims dm;
-    return make_dims(shape, &dm, GMA_OP_RESPONSIBILITIES) == GMA_OK ? plan_balance(dm).bytes : 0;
+    return balance_dims(shape, &dm) == GMA_OK ? plan_balance(dm).bytes : 0;
 }
 
 extern "C" gma_status gma_balance_loss(const gma_shape *shape, gma_params params, const void *x, const int *lengths,
@@ -1193,7 +1200,7 @@ extern "C" gma_status gma_balance_loss(const gma_shape *shape, gma_params params
 {
     GMA_TRY(take_timeout());
     Dims dm;
-    GMA_TRY(make_dims(shape, &dm, GMA_OP_RESPONSIBILITIES));
+    GMA_TRY(balance_dims(shape, &dm));
     GMA_TRY(check_params(params));
     GMA_TRY(check_ptr(x, dm.N > 0));
     GMA_TRY(check_ptr(gamma, dm.N > 0));
@@ -1239,7 +1246,7 @@ extern "C" gma_status gma_balance_backward(const gma_shape *shape, gma_params pa
 {
     GMA_TRY(take_timeout());
     Dims dm;
-    GMA_TRY(make_dims(shape, &dm, GMA_OP_RESPONSIBILITIES));
+    GMA_TRY(balance_dims(shape, &dm));
     if (accumulate != 0 && accumulate != 1) return GMA_ERR_INVALID_ARG;
     GMA_TRY(check_params(params));
     const bool any = dm.N > 0;

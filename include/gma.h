@@ -359,9 +359,9 @@ gma_status gma_beam_reorder(int B, int W, size_t row_bytes, const int *parent, v
  * heads whose rows are all but one-hot keep their relative accuracy, down to
  * the end of the fp32 range (posteriors below 2^-126 are 0).
  * A row with a NaN makes prob and loss NaN and is counted nowhere.
- * Sums run in a fixed order: repeated calls give identical results.  Workspace:
- * gma_balance_workspace_size(shape); shape->d_v, chunk, eps, v_dtype and
- * gemm_dtype are checked but unused.                                        */
+ * Sums run in a fixed order: repeated calls give identical results.  N <= 2^30.
+ * Workspace: gma_balance_workspace_size(shape); shape->d_v, chunk, eps, v_dtype
+ * and gemm_dtype are checked but unused.                                    */
 size_t gma_balance_workspace_size(const gma_shape *shape);
 gma_status gma_balance_loss(const gma_shape *shape, gma_params params, const void *x,
                             const int *lengths, float *gamma, float *loss, long long *counts,

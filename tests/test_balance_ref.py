@@ -120,3 +120,15 @@ def test_binding_refuses_host_tensors():
         gma.gma_balance_loss(s, *p, z(1, 1, 4, 16), z(1, 1, 4, 2), z(1), z(1, 2), z(1, 2))
     with pytest.raises(TypeError, match="CUDA tensor"):
         gma.gma_balance_backward(s, *p, z(1, 1, 4, 16), z(1, 1, 4, 2), z(1, 2), z(1), *p, z(1))
+
+
+@pytest.mark.parametrize("N", [(1 << 30) + 1, (1 << 31) - 200, (1 << 31) - 1])
+def test_rejects_sequences_whose_positions_would_pass_31_bits(lib, N):
+    s = _shape(B=1, H=1, N=N, d_route=16, d_v=16, K=2)
+    assert gma.gma_balance_workspace_size(s) == 0
+    for names in (FWD, BWD):
+        assert _call(lib, names, s) == 2
+    s.N = 1 << 30   # passes the shape's checks (the parameter's alignment is what fails)
+    assert gma.gma_balance_workspace_size(s) > 0
+    for names in (FWD, BWD):
+        assert _call(lib, names, s, mu=_at("mu") + 4) == 3
