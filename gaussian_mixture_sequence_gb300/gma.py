@@ -494,6 +494,9 @@ def _p(t, name, shape, dtype, dev, optional=False):
     if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == shape
             and t.is_contiguous()):
         return t.data_ptr()   # 0 where it is empty
+    if isinstance(t, torch.Tensor) and t.numel() == 0 and 0 not in shape:
+        # (_ptr would take it for none: lengths or a state that a caller gave would have no say)
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return _ptr(t, name, shape, dtype, torch.device("cuda", dev), optional)
 
 
