@@ -7,6 +7,7 @@
 namespace gma {
 namespace {
 
+// Knuth's sum of two values and its error, and Dekker's for ordered ones.
 __device__ __forceinline__ float2 two_sum(float a, float b)
 {
     const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
@@ -24,7 +25,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
 }
 
 // Logarithms and exponentials to about 2^-30, as sums of two fp32 values.
-constexpr float kLn2Hi = 0.693359375f, kLn2Lo = -2.12194440054690581e-4f;   // ln 2 = hi + lo, hi of 9 bits
+// Cody and Waite's split: ln 2 = hi + lo, hi = 355 / 512 of 9 bits, so that n hi is exact.
+constexpr float kLn2Hi = 0.693359375f, kLn2Lo = -2.12194440054690581e-4f;
 
 __device__ __forceinline__ float2 div2(float2 a, float2 b)
 {

@@ -1,6 +1,6 @@
 // Responsibilities (S1) on the tensor cores for 17 <= K <= 512 components (K = 128
-// has the bounded routing of its own) and d_route = 64: every log-joint of every row,
-// for any inputs.
+// has the bounded routing of its own, but for the balance loss) and d_route = 64: every
+// log-joint of every row, for any inputs.
 //
 // The posterior of the GMA explainer ("핵심 메커니즘": gamma_ik = p(z = k | x_i)
 // under the diagonal GMM) is a softmax over the log-joints

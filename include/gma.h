@@ -248,7 +248,8 @@ gma_status gma_decode_step(const gma_shape *shape, gma_params params, const void
  *                 sequence.  May be state_in itself.
  * Supported: 1 <= D <= 65536, N <= 2^30, B*H <= 65535, B*H*N*D < 2^40.  With
  * N = 0 the sequence pointers may be NULL and state_out is state_in (or 0).  A
- * NaN gate or input makes its channel NaN from there on.  No workspace.     */
+ * NaN gate or input makes its channel NaN from there on, an infinite one
+ * infinite or NaN.  An a_t below 2^-125 counts as 2^-125.  No workspace.    */
 typedef enum { GMA_SCAN_SUM = 0, GMA_SCAN_MEAN = 1 } gma_scan_form;
 
 typedef struct {
@@ -267,7 +268,9 @@ gma_status gma_gated_scan(const gma_scan_shape *shape, const void *x, const void
  *           = lambda_t (1 - a_t)                (MEAN)
  *   dgate_t = lambda_t h_{t-1} a_t (1 - a_t)    (SUM; MEAN: h_{t-1} - x_t)
  *   dstate_in = a_1 lambda_1
- *   out         the forward's output (h_{t-1} is read from it as it was stored)
+ *   out         the forward's output (h_{t-1} is read from it as it was stored:
+ *               in bf16, dgate carries that rounding beside its own, and in the
+ *               MEAN form relative to h_{t-1} rather than to the difference)
  *   dout        [B, H, N, D] (dtype): dL/dout
  *   dstate_out  nullable [B, H, D] fp32: dL/dstate_out (NULL: 0)
  *   dx, dgate   [B, H, N, D] (dtype), overwritten; 0 behind a sequence
@@ -360,8 +363,9 @@ gma_status gma_beam_reorder(int B, int W, size_t row_bytes, const int *parent, v
  * the end of the fp32 range (posteriors below 2^-126 are 0).
  * A row with a NaN makes prob and loss NaN and is counted nowhere.
  * Sums run in a fixed order: repeated calls give identical results.  N <= 2^30.
- * Workspace: gma_balance_workspace_size(shape); shape->d_v, chunk, eps, v_dtype
- * and gemm_dtype are checked but unused.                                    */
+ * Workspace: gma_balance_workspace_size(shape) for this call as for the
+ * gradients, whose lists of terms take 8 B*H*N*K bytes of it (twice gamma).
+ * shape->d_v, chunk, eps, v_dtype and gemm_dtype are checked but unused.    */
 size_t gma_balance_workspace_size(const gma_shape *shape);
 gma_status gma_balance_loss(const gma_shape *shape, gma_params params, const void *x,
                             const int *lengths, float *gamma, float *loss, long long *counts,
@@ -379,7 +383,8 @@ gma_status gma_balance_loss(const gma_shape *shape, gma_params params, const voi
  * gma_backward: overwritten (0 behind a sequence) where accumulate = 0, added
  * to where accumulate = 1, so that the loss's gradients join those of the
  * mixer.  In a row, terms below 2^-24 of its largest delta (2^-17 / K of it
- * where K > 128) are left out.  Same workspace size.                        */
+ * where K > 128) are left out.  Counts enter as fp32 values: differences of
+ * them are exact below 2^24.  Same workspace size.                          */
 gma_status gma_balance_backward(const gma_shape *shape, gma_params params, const void *x,
                                 const int *lengths, const float *gamma, const long long *counts,
                                 const float *dloss, float *dx, float *dmu, float *dvar_raw,
