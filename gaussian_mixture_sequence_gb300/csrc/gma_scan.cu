@@ -38,8 +38,9 @@ __device__ __forceinline__ float rcp_approx(float x)
 
 // a = sigmoid(g) and r = 1 - a = sigmoid(-g).  With e = exp(-g): a = 1 / (1 + e), r = e a,
 // which keeps the relative accuracy of both ends (1 - a would lose r for large gates) but for
-// the rounding of g log2 e, about |g| units of 2^-24 on the smaller of the two.  The exponent is held below 125 powers of two, where 1 / (1 + e) is still a normal number; a NaN
-// gate stays NaN.
+// the rounding of g log2 e, about |g| units of 2^-24 on the smaller of the two.  The exponent
+// is held below 125 powers of two, where 1 / (1 + e) is still a normal number; a NaN gate stays
+// NaN.
 __device__ __forceinline__ void gate_of(float g, float &a, float &r)
 {
     const float e = ex2_approx(min_nan(g * -1.4426950408889634f, 125.f));
