@@ -2,7 +2,7 @@
 // The operations are those of the GMA explainer "Gaussian Mixture Attention:
 // Linear-Time Sequence Mixing via Probabilistic Latent Routing" (technical
 // summary, "핵심 메커니즘" and "변형 및 학습"); see include/gma.h.
-#include "gma_internal.cuh"
+#include "gma_operators.cuh"
 
 #include <math.h>
 

@@ -9,7 +9,7 @@
 // head's scale (the largest second-best posterior among some of its rows) is evaluated again, a few per
 // row, as unevaluated sums of two fp32 values (about 2^-45 of the sum; the FP64 pipe of this GPU is far
 // too slow for it).
-#include "gma_internal.cuh"
+#include "gma_operators.cuh"
 #include "gma_pair.cuh"
 
 #include <float.h>

@@ -6,7 +6,7 @@
 // a running maximum and sum per thread (for lse) and the W largest logits of the row's part.  The parts
 // of each row and then the W rows of a request are joined by the first CTA of a cluster that holds all
 // parts of a request, where they are few, or by a second, small kernel.
-#include "gma_internal.cuh"
+#include "gma_operators.cuh"
 #include "gma_pair.cuh"
 
 #include <cooperative_groups.h>

@@ -37,7 +37,7 @@
 // the squares (even): in ascending order some odd steps were measured to take W
 // from the step before them (the products of the first tile of a CTA were exact,
 // later ones not), and in this order every product matches its fp64 terms.
-#include "gma_internal.cuh"
+#include "gma_operators.cuh"
 #include "gma_tc.cuh"
 
 #include <float.h>

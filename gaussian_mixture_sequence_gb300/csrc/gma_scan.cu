@@ -9,7 +9,7 @@
 // a_t and U the recurrence started at 0, and (A2, U2) after (A1, U1) is (A2 A1, A2 U1 + U2).
 // The gradient runs the same composition backwards in time: c_t = a_t (dout_t + c_{t+1})
 // is what lambda_t = dout_t + c_{t+1} hands to the row before.
-#include "gma_internal.cuh"
+#include "gma_operators.cuh"
 #include "gma_tc.cuh"
 
 #include <type_traits>

@@ -1,5 +1,5 @@
 // Tensor maps for TMA (bulk tensor) loads, encoded on the host.
-#include "gma_internal.cuh"
+#include "gma_operators.cuh"
 
 #include <string.h>
 

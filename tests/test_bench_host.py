@@ -225,3 +225,13 @@ def test_small_k_routing_roofline():
     assert not bench.tc_routing(W["causal_4k"])
     assert bench.stage_work("resp_q", W["causal_8k_K512"].with_(K=520))[1] == "alu"
     assert bench.stage_work("resp_q", W["causal_8k_K256"].with_(d=128))[1] == "alu"
+
+
+def test_declaring_an_operator_drops_no_counters():
+    """The launchers of the operators around the mixer are declared apart from the headers whose contents
+    key the counters, so that the headline keeps its measured traffic when one is added or changed."""
+    csrc = os.path.join(bench.ROOT, "gaussian_mixture_sequence_gb300", "csrc")
+    names = ("launch_scan_fwd", "launch_beam_select", "launch_balance_loss")
+    keyed = "".join(open(os.path.join(csrc, f)).read() for f in ("gma_internal.cuh", "gma_tc.cuh"))
+    declared = open(os.path.join(csrc, "gma_operators.cuh")).read()
+    assert all(n in declared and n not in keyed for n in names)
